@@ -4,17 +4,21 @@
 //   h = rnd(x + residual)            rnd: to the tensors' own type, so that the norm sees exactly
 //                                    what the residual stream carries on
 //   y = h / sqrt(mean(h^2) + eps) (offset + w)
-//   per block: s = max(max |y|, 2^-100) / F,  q = rnd8(y (1/s)),  F = 448 (e4m3) or 57344 (e5m2)
-// Sums and products in fp32; the roundings are those of h, of s and 1/s, and of q to nearest even,
-// saturating. The floor of 2^-100 keeps s and 1/s finite for blocks of zeros.
+//   per block: s = max(max |y|, 2^-100) / F,  q = rnd8(y / s),  F = 448 (e4m3) or 57344 (e5m2)
+// Sums and products in fp32; q to nearest even, saturating. bf16 values often lie halfway between
+// two codes, and any rounding on the way tips them: y / s is formed as y F / max with F / max as a
+// float pair, so that what is rounded to a code is the quotient rounded to fp32 once. In the norm
+// 1 / sqrt(mean + eps) divides out of it but for a power of two, so the codes do not see its rounding
+// either (only that of h (offset + w)). The floor of 2^-100 keeps s and 1/s finite for blocks of zeros.
 //
 // Both kernels touch each byte once. The table's quantisation is bound by memory (262144 x 2816 bf16:
-// 346 us, 6.4 TB/s). The norm is too where a row is a warp's (65536 x 256 fp32: 35 us, 6.3 TB/s);
+// 324 us, 6.8 TB/s). The norm is too where a row is a warp's (65536 x 256 fp32: 36 us, 6.1 TB/s);
 // longer rows pay for the sum across warps and about 30 instructions a value (65536 x 2816 bf16 with
-// a residual: 254 us, 5.1 TB/s; 16001 x 5000: 138 us, 4.1 TB/s; one row: 2.3 us).
+// a residual: 257 us, 5.0 TB/s; 16001 x 5000: 121 us, 4.6 TB/s; one row: 2.3 us).
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ds_head.h"
 
@@ -98,26 +102,45 @@ DS_DEV Raw8<T> round8(float (&f)[8]) {
   return t;
 }
 
-// max / F correctly rounded: the product with 1 / F and one step on its remainder.
-DS_DEV float block_scale(float amax, float top, float rtop) {
-  const float m = fmaxf(amax, kTinyMax), s = m * rtop;
-  const float r = __fmaf_rn(-s, top, m);
-  return isinf(m) ? m : __fmaf_rn(r, rtop, s);
+// F / m as a float pair: good to 2^-44 of itself, which is the remainder's own rounding.
+struct Factor {
+  float hi, lo;
+};
+DS_DEV Factor block_factor(float m, float top) {
+  const float r = __frcp_rn(m), hi = top * r;
+  return Factor{hi, isinf(m) ? 0.f : __fmaf_rn(-hi, m, top) * r};
 }
 
-// Codes of y * inv in columns c .. c + 7 of a row of n codes; VEC: the row is 8-byte aligned.
-template <bool VEC>
-DS_DEV void store_codes(uint8_t* row, int c, int n, const float (&y)[8], float inv,
-                        __nv_fp8_interpretation_t kind) {
-  uint32_t w[2];
+// Two products, or two multiply-adds, in one instruction: what issues is what these kernels wait for.
+DS_DEV float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n"
+      " mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+DS_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// Codes of y * f in columns c .. c + 7 of a row of n codes; VEC: the row is 8-byte aligned.
+template <bool VEC, bool E5M2>
+DS_DEV void store_codes(uint8_t* row, int c, int n, const float (&y)[8], const Factor f) {
+  constexpr __nv_fp8_interpretation_t kind = E5M2 ? __NV_E5M2 : __NV_E4M3;
+  uint32_t p[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-        make_float2(y[4 * h] * inv, y[4 * h + 1] * inv), __NV_SATFINITE, kind);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-        make_float2(y[4 * h + 2] * inv, y[4 * h + 3] * inv), __NV_SATFINITE, kind);
-    w[h] = lo | (hi << 16);
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = make_float2(y[2 * i], y[2 * i + 1]);
+    const float2 v = fma2(x, make_float2(f.hi, f.hi), mul2(x, make_float2(f.lo, f.lo)));
+    p[i] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, kind);
   }
+  const uint32_t w[2] = {p[0] | (p[1] << 16), p[2] | (p[3] << 16)};
   if (VEC && c + 8 <= n) {
     *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
   } else {
@@ -152,8 +175,9 @@ struct NormArgs {
 // lanes), blockDim.y rows a CTA at a time. A row stays in registers between the sum of squares and
 // the output, NV groups of 8 columns a thread, all of whose loads are in flight at once; the weight
 // stays there over all rows of the CTA, and the next row is fetched meanwhile (NV <= 2).
-template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) k_rmsnorm_fp8(const NormArgs a) {
+template <typename T, bool VEC, int NV, bool E5M2>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : (NV == 2 ? 384 : 512), NV == 2 ? 2 : 1)
+    k_rmsnorm_fp8(const NormArgs a) {
   __shared__ float part[2][32];
   pdl_wait();
   const int tpr = blockDim.x, d = a.d, wpr = tpr >> 5, w0 = threadIdx.y * wpr;
@@ -170,7 +194,6 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) k_rmsnorm_fp8(const Norm
 #pragma unroll
     for (int j = 0; j < NV; ++j) weight(j, g[j]);
   }
-  const __nv_fp8_interpretation_t kind = a.e5m2 ? __NV_E5M2 : __NV_E4M3;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   int64_t r0 = (int64_t)blockIdx.x * blockDim.y;
   Raw8<T> t[NV], res[NV];
@@ -217,7 +240,12 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) k_rmsnorm_fp8(const Norm
       ss = warp_sum(lane < wpr ? part[turn & 1][w0 + lane] : 0.f);
     }
     if (!live) continue;
+    // 1 / sqrt(mean + eps) = r2 t, r2 a power of two (or 0, inf or NaN, with t = 1)
     const float rinv = 1.0f / sqrtf(ss * a.rd + a.eps);
+    const uint32_t rb = __float_as_uint(rinv);
+    const float r2 = isnan(rinv) ? rinv : __uint_as_float(rb & 0x7f800000u);
+    const float t1 = __uint_as_float((rb & 0x007fffffu) | 0x3f800000u);
+    const float least = __fdividef(kTinyMax, t1);  // the floor of max |y|, over t
     uint8_t* q = a.q + r * a.q_stride;
     float* scales = a.scales + r * a.s_stride;
 #pragma unroll
@@ -226,10 +254,14 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) k_rmsnorm_fp8(const Norm
       if constexpr (!KEEP) weight(j, g[0]);
       float (&w)[8] = g[KEEP ? j : 0];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * rinv * w[i];
-      const float s = block_scale(amax16(h[j]), a.top, a.rtop);
-      if ((threadIdx.x & 15) == 0 && c < d) scales[c / kScaleBlock] = s;
-      if (c < d) store_codes<VEC>(q, c, d, h[j], __frcp_rn(s), kind);
+      for (int i = 0; i < 8; i += 2) {  // y / t1
+        const float2 v = mul2(mul2(make_float2(h[j][i], h[j][i + 1]), make_float2(r2, r2)),
+                              make_float2(w[i], w[i + 1]));
+        h[j][i] = v.x, h[j][i + 1] = v.y;
+      }
+      const float m = amax16(h[j]);
+      if ((threadIdx.x & 15) == 0 && c < d) scales[c / kScaleBlock] = fmaxf(m * t1, kTinyMax) * a.rtop;
+      if (c < d) store_codes<VEC, E5M2>(q, c, d, h[j], block_factor(fmaxf(m, least), a.top));
     }
   }
 }
@@ -240,7 +272,7 @@ struct QuantArgs {
   float* scales;
   int64_t rows, x_stride, q_stride, s_stride;
   int cols;
-  float top, rtop;
+  float top;
   int e5m2;
 };
 
@@ -260,14 +292,13 @@ DS_DEV float amax8(const Raw8<T>& t) {
 }
 
 // One 128 x 128 block a CTA of 256 threads: 16 threads across, 16 rows at a time, 8 loads of 8
-// columns in flight a thread. ROWS: each row of the block has its own scale. Blocks go to CTAs
+// columns in flight a thread, four CTAs an SM for bf16 (262144 x 2816: 324 us; three, 354). ROWS: each row of the block has its own scale. Blocks go to CTAs
 // along the rows of x, so that the CTAs that run together read whole rows.
-template <typename T, bool VEC, bool ROWS>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_quantize_fp8(const QuantArgs a) {
+template <typename T, bool VEC, bool ROWS, bool E5M2>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) k_quantize_fp8(const QuantArgs a) {
   __shared__ float part[8];
   pdl_wait();
   const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
-  const __nv_fp8_interpretation_t kind = a.e5m2 ? __NV_E5M2 : __NV_E4M3;
   const int64_t ncb = ((int64_t)a.cols + kScaleBlock - 1) / kScaleBlock;
   const int64_t n = ncb * ((a.rows + kScaleBlock - 1) / kScaleBlock);
   for (int64_t blk = blockIdx.x; blk < n; blk += gridDim.x) {
@@ -280,7 +311,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_quantize_fp8(co
       const int64_t r = r0 + ry + 16 * i;
       v[i] = load8<T, VEC>(static_cast<const T*>(a.x) + r * a.x_stride, r < a.rows ? c : a.cols, a.cols);
     }
-    float s = 0.f, inv = 0.f;
+    Factor f{};
     if constexpr (!ROWS) {
       float m = 0.f;
 #pragma unroll
@@ -292,9 +323,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_quantize_fp8(co
       __syncthreads();
 #pragma unroll
       for (int w = 0; w < 8; ++w) m = fmaxf(m, part[w]);
-      s = block_scale(m, a.top, a.rtop);
-      inv = __frcp_rn(s);
-      if (threadIdx.x == 0) a.scales[rb * a.s_stride + cb] = s;
+      m = fmaxf(m, kTinyMax);
+      f = block_factor(m, a.top);
+      if (threadIdx.x == 0) a.scales[rb * a.s_stride + cb] = __fdiv_rn(m, a.top);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -303,14 +334,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_quantize_fp8(co
         float m = amax8(v[i]);
 #pragma unroll
         for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        s = block_scale(m, a.top, a.rtop);
-        inv = __frcp_rn(s);
-        if (cx == 0 && r < a.rows) a.scales[r * a.s_stride + cb] = s;
+        m = fmaxf(m, kTinyMax);
+        f = block_factor(m, a.top);
+        if (cx == 0 && r < a.rows) a.scales[r * a.s_stride + cb] = __fdiv_rn(m, a.top);
       }
       if (r < a.rows && c < a.cols) {
         float y[8];
         unpack8(v[i], y);
-        store_codes<VEC>(a.q + r * a.q_stride, c, a.cols, y, inv, kind);
+        store_codes<VEC, E5M2>(a.q + r * a.q_stride, c, a.cols, y, f);
       }
     }
   }
@@ -326,10 +357,13 @@ float top_of(int fp8) { return fp8 == DS_FP8_E5M2 ? 57344.f : 448.f; }
 
 template <typename T, bool VEC>
 cudaError_t norm_nv(int nv, dim3 grid, dim3 block, cudaStream_t st, const NormArgs& n) {
-  if (nv == 1) return launch_k(k_rmsnorm_fp8<T, VEC, 1>, grid, block, 0, st, n);
-  if (nv == 2) return launch_k(k_rmsnorm_fp8<T, VEC, 2>, grid, block, 0, st, n);
-  if (nv == 4) return launch_k(k_rmsnorm_fp8<T, VEC, 4>, grid, block, 0, st, n);
-  return launch_k(k_rmsnorm_fp8<T, VEC, 8>, grid, block, 0, st, n);
+  auto go = [&](auto e4m3, auto e5m2) {
+    return launch_k(n.e5m2 ? e5m2 : e4m3, grid, block, 0, st, n);
+  };
+  if (nv == 1) return go(k_rmsnorm_fp8<T, VEC, 1, false>, k_rmsnorm_fp8<T, VEC, 1, true>);
+  if (nv == 2) return go(k_rmsnorm_fp8<T, VEC, 2, false>, k_rmsnorm_fp8<T, VEC, 2, true>);
+  if (nv == 4) return go(k_rmsnorm_fp8<T, VEC, 4, false>, k_rmsnorm_fp8<T, VEC, 4, true>);
+  return go(k_rmsnorm_fp8<T, VEC, 8, false>, k_rmsnorm_fp8<T, VEC, 8, true>);
 }
 
 }  // namespace
@@ -343,9 +377,10 @@ cudaError_t launch_rmsnorm_fp8(const ds_rmsnorm_fp8_args& a, cudaStream_t st) {
                    (!a.h || on16(a.h, a.h_stride * es)) && on16(a.weight, 0) && on8(a.q, a.q_stride);
   const int groups = (a.d + 7) / 8;
   // Groups of 8 columns a thread: one, unless a row then takes 513 to 768 threads, of which an SM
-  // holds one row only (at 64 registers a thread): two then, and three rows. Measured, bf16 with a
-  // residual, one / two groups: 65536 x 2816 254 / 369 us, 16384 x 8192 166 / 199 us, 16001 x 5000
-  // 187 / 138 us. More where a row has more than 8192 columns.
+  // holds one row only (at 64 registers a thread): two then, and two rows (at 80). Measured, bf16
+  // with a residual, one group: 65536 x 2816 257 us, 16384 x 8192 169 us, 16001 x 5000 187 us; two:
+  // 16001 x 5000 121 us (one row an SM, 128 registers: 140). More where a row has more than 8192
+  // columns.
   int nv = groups > 512 && groups <= 768 ? 2 : 1;
   if (groups > 1024)
     for (nv = 4; nv * 512 < groups;) nv *= 2;
@@ -356,7 +391,7 @@ cudaError_t launch_rmsnorm_fp8(const ds_rmsnorm_fp8_args& a, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // CTAs that fit the GPU at once, each over its share of the rows
-  const int64_t fit = (int64_t)sms * std::max(1, (nv == 1 ? 1024 : 2048) / (tpr * rpc));
+  const int64_t fit = (int64_t)sms * std::max(1, (nv == 1 ? 1024 : (nv == 2 ? 768 : 2048)) / (tpr * rpc));
   const dim3 block(tpr, rpc), grid((unsigned)std::min<int64_t>((a.rows + rpc - 1) / rpc, fit));
   if (es == 4)
     return vec ? norm_nv<float, true>(nv, grid, block, st, n)
@@ -368,19 +403,22 @@ cudaError_t launch_rmsnorm_fp8(const ds_rmsnorm_fp8_args& a, cudaStream_t st) {
 cudaError_t launch_quantize_fp8(const ds_quantize_fp8_args& a, cudaStream_t st) {
   const int es = a.dtype == DS_DTYPE_FP32 ? 4 : 2;
   QuantArgs n{a.x, a.q, a.scales, a.rows, a.x_stride, a.q_stride, a.scales_stride, a.cols,
-              top_of(a.fp8), 1.f / top_of(a.fp8), a.fp8 == DS_FP8_E5M2};
+              top_of(a.fp8), a.fp8 == DS_FP8_E5M2};
   const bool vec = on16(a.x, a.x_stride * es) && on8(a.q, a.q_stride);
   const int64_t blocks = ((int64_t)a.cols + kScaleBlock - 1) / kScaleBlock *
                          ((a.rows + kScaleBlock - 1) / kScaleBlock);
   const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 30));
-  auto go = [&](auto k) { return launch_k(k, grid, dim3(256), 0, st, n); };
-  const bool rows = a.block_rows == 1;
-  if (es == 4)
-    return vec ? (rows ? go(k_quantize_fp8<float, true, true>) : go(k_quantize_fp8<float, true, false>))
-               : (rows ? go(k_quantize_fp8<float, false, true>) : go(k_quantize_fp8<float, false, false>));
-  using B = __nv_bfloat16;
-  return vec ? (rows ? go(k_quantize_fp8<B, true, true>) : go(k_quantize_fp8<B, true, false>))
-             : (rows ? go(k_quantize_fp8<B, false, true>) : go(k_quantize_fp8<B, false, false>));
+  auto go = [&](auto e4m3, auto e5m2) {
+    return launch_k(n.e5m2 ? e5m2 : e4m3, grid, dim3(256), 0, st, n);
+  };
+  auto pick = [&](auto t, auto v) {
+    using T = decltype(t);
+    constexpr bool V = decltype(v)::value;
+    return a.block_rows == 1 ? go(k_quantize_fp8<T, V, true, false>, k_quantize_fp8<T, V, true, true>)
+                             : go(k_quantize_fp8<T, V, false, false>, k_quantize_fp8<T, V, false, true>);
+  };
+  if (es == 4) return vec ? pick(float{}, std::true_type{}) : pick(float{}, std::false_type{});
+  return vec ? pick(__nv_bfloat16{}, std::true_type{}) : pick(__nv_bfloat16{}, std::false_type{});
 }
 
 }  // namespace ds

@@ -421,8 +421,9 @@ enum { DS_FP8_E4M3 = 0, DS_FP8_E5M2 = 1 };
 /* Norm with 8-bit rows. For each row:
  *   h = x + residual, rounded to dtype (h = x when residual is NULL);
  *   y = h / sqrt(mean(h^2) + eps) * (weight_offset + weight);
- *   for each 128 columns: scale = max(max |y|, 2^-100) / F, q = y * (1 / scale) rounded to the
- *   nearest code (ties to even), saturating.
+ *   for each 128 columns: scale = max(max |y|, 2^-100) / F, q = y / scale rounded to fp32 and then to
+ *   the nearest code (ties to even), saturating. The codes see no other rounding than this and that
+ *   of h * (weight_offset + weight) to fp32; a scale is good to 2^-18.
  * Sums and products are fp32 (so |h| above 1.8e19 overflows the mean). A NaN in y becomes a NaN
  * code and does not enter the scale.
  *   rows, d         [rows, d]; 0 <= rows <= 2^30, 1 <= d <= 32768 (else DS_ERR_UNSUPPORTED)
