@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const int half = (warp - 4) >> 2;  // column half of the tile
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     const uint32_t stg0 = sbase + T::kStages * T::kStage + (uint32_t)(warp - 4) * T::kStg;
-    int buf = 0;
+    int buf = 0, box = 0;  // box: of the output boxes, the next one
     uint32_t bphase = 0;
     bool ok = true;
     for (int tile = unit; tile < n_tiles && ok; tile += n_units) {
@@ -383,10 +383,13 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 #pragma unroll
       for (int bx = 0; bx < COLS / 32; ++bx) {
         if (tma_out) {
-          // boxes are used in turn: the one before last has been read when all but the last have
+          // boxes are used in turn, over all tiles of this warp (a tile of 64 columns has one a warp):
+          // the one before last has been read when all but the last have
           constexpr uint32_t kBox = sizeof(O) * 1024;
           constexpr int kBoxes = T::kStg / kBox;
-          const uint32_t stg = stg0 + (uint32_t)(bx % kBoxes) * kBox;
+          static_assert(kBoxes == 1 || kBoxes == 2, "the wait below is for one or two boxes");
+          const uint32_t stg = stg0 + (COLS / 32 % kBoxes == 0 ? bx % kBoxes : box) * kBox;
+          box = (box + 1) % kBoxes;
           if (lane == 0) {
             if constexpr (kBoxes == 2) bulk_wait_read_le1();
             else bulk_wait_read_all();

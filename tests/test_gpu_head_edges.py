@@ -1,4 +1,5 @@
-"""The 8-bit output head where it can go wrong: values halfway between two codes."""
+"""The 8-bit output head where it can go wrong: values halfway between two codes, products of several
+tiles a CTA."""
 import numpy as np
 import pytest
 import torch
@@ -82,3 +83,36 @@ def test_codes_of_a_norm_see_one_rounding(dt, fmt, R, d):
         a, b = O.fp8_round(v / slack, fmt), O.fp8_round(v * slack, fmt)
         assert np.all((got == a) | (got == b))
         assert np.mean(a != b) < 1e-2  # nearly every code is pinned to one value (ties to two)
+
+
+# ------------------------------------------------------------------------------------- product
+def operands(m, n, k, seed):
+    """Codes and scales of an A [m, k] and a B [n, k]."""
+    g = gen(seed)
+    cols = -(-k // 16) * 16
+    code = lambda r: (torch.randn(r, cols, device="cuda", generator=g) * 100).clamp(-400, 400).to(  # noqa: E731
+        torch.float8_e4m3fn)[:, :k]
+    scale = lambda r: torch.exp(torch.randn(r, -(-k // 128), device="cuda", generator=g)) / 100  # noqa: E731
+    return code(m), scale(m), code(n), scale(-(-n // 128))
+
+
+# with 152 SMs: the first five have two and more 64-column tiles a CTA, the next three 128-column
+# ones, the last 256-column ones of CTA pairs
+@pytest.mark.parametrize("m,n,k", [(300, 6464, 128), (1409, 1600, 128), (20000, 64, 128), (25000, 120, 160),
+                                   (640, 7688, 256), (40000, 128, 128), (300, 14000, 128), (1409, 3200, 128),
+                                   (1409, 12000, 128)])
+def test_products_of_several_tiles_a_cta(m, n, k):
+    """The same sums leave in both types: the bf16 product is the fp32 one rounded."""
+    for seed in range(3):
+        ops = operands(m, n, k, seed)
+        full = head.matmul_fp8(*ops, out_dtype="fp32")
+        for _ in range(3):
+            out = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+            assert torch.equal(head.matmul_fp8(*ops, out=out), full.bfloat16())
+    # and the fp32 ones are the definition's: sums of 128 products cut to no worse than 2^-23 of their
+    # absolute terms each, one addition a block, half a step of the output
+    rows = torch.arange(0, m, max(1, m // 50), device="cuda")
+    want, mag = O.matmul(f64(ops[0][rows]), f64(ops[1][rows]), f64(ops[2]), f64(ops[3]))
+    bound = (128 + ops[1].shape[1]) * 2.0 ** -23 * mag
+    assert np.all(np.abs(f64(full[rows]) - want) <= bound + 2.0 ** -24 * (np.abs(want) + bound))
+    assert head.head_status() == 0
