@@ -1386,7 +1386,7 @@ struct Sampler {
       if (by_k) keep = cut_by_number(keep, (uint64_t)k);
       if (by_p) {
         const float p[3] = {-INFINITY, -INFINITY, -INFINITY};
-        if (!list && !odd) z = pass<false, true, 1>(keep, p);
+        if ((!list || by_k) && !odd) z = pass<false, true, 1>(keep, p);  // (else taken with the list)
         bool within = false;  // all that min_p keeps has less than top_p of the mass
         if (floor_l > keep.cut && !odd) {
           const Sums s = pass<false, true, 1>(Kept{floor_l, INT_MAX}, p);

@@ -116,3 +116,24 @@ def test_products_of_several_tiles_a_cta(m, n, k):
     bound = (128 + ops[1].shape[1]) * 2.0 ** -23 * mag
     assert np.all(np.abs(f64(full[rows]) - want) <= bound + 2.0 ** -24 * (np.abs(want) + bound))
     assert head.head_status() == 0
+
+
+# ------------------------------------------------------------------------------------- sampling
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("R", [2, 400])
+def test_sampling_with_thousands_of_ties_at_the_kth_logit(dt, R):
+    """The list overflows, and top-p is a share of the first k tokens, the lowest indices of the tie."""
+    V, k = 20011, 50
+    g = gen(R)
+    logits = torch.randn(R, V, device="cuda", generator=g).clamp(max=0.25)
+    logits[:, 7000] = 1.5
+    logits = logits.to(DT[dt])
+    u = torch.rand(R, device="cuda", generator=g)
+    full = lambda v, t=torch.float32: torch.full((R,), v, dtype=t, device="cuda")  # noqa: E731
+    for p in (0.77, 0.3):
+        token, prob = head.sample_logits(logits, u, top_k=full(k, torch.int32), top_p=full(p))
+        for r in range(0, R, max(1, R // 20)):
+            want, pw, margin = O.sample_row(f64(logits[r]), float(u[r]), top_k=k,
+                                            top_p=float(np.float32(p)))
+            assert margin > 2.0 ** -24 and int(token[r]) == want
+            assert abs(float(prob[r]) - pw) <= 2.0 ** -20 * pw
