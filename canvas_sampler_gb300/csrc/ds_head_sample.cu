@@ -63,7 +63,8 @@ cudaError_t launch_sample_logits(const ds_sample_logits_args& a, cudaStream_t st
   int lg = 0;
   while ((1ll << lg) < a.vocab) ++lg;
   SampleArgs s{a.logits, a.temperature, a.top_p, a.min_p, a.u, a.top_k, a.done, a.token, a.prob,
-               a.logits_stride, a.rows, (int)a.vocab, 0, ldexpf(1.f, 61 - lg)};
+               a.logits_stride, a.rows, (int)a.vocab, 0, ldexpf(1.f, kMassBits - lg),
+               std::max(0, kListBits - (kMassBits - lg))};
   // rows in slices of what a grid holds
   const int64_t most = 1ll << 27;
   for (int64_t r0 = 0; r0 < a.rows; r0 += most) {

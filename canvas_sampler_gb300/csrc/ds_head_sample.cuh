@@ -9,11 +9,14 @@
 // is {l > cut, or l == cut and index <= tie}.
 //
 // The answer is a whole number, and it is the one of the definition: a mass is a sum of integers (w
-// scaled by a power of two, so the order of summation does not matter). Two weights are used. The
+// in units of a power of two, so the order of summation does not matter). Two weights are used. The
 // exact one (weight_pair) is good to about 2^-37 without 64-bit floats, of which this machine has
 // few. The quick one is a single special-function exponential, and a mass of quick weights comes
 // with a bound on its error; where a decision (a border of top-p, the token itself) lies within
-// that bound, the mass is taken again from exact weights.
+// that bound, the mass is taken again from exact weights. The unit of an exact mass is 2^-60 to 2^-61
+// of it, as a quick pass before has told (refine), or 2^-50 of the largest weight in a list of 2048:
+// what rounding n weights to whole units drops, n / 2 units, is below 2^-37 of the mass for any n up
+// to 2^24. (In units that fit any row of 2^24 tokens it would be 2^-14 of a heavy token's.)
 //
 // One row a cluster of up to 8 CTAs, each with a contiguous share of the vocabulary in its shared
 // memory, read from memory once (rows too long for that are read again in each pass). Each warp
@@ -59,13 +62,22 @@ struct SampleArgs {
   int vocab;
   int chunk;   // vocabulary entries per CTA (a multiple of 16 bytes of them), from the aligned-down
                // start of the row
-  float unit;  // weights are counted in units of 1 / unit (a power of two; the sum fits 62 bits)
+  float unit;  // weights are counted in units of 1 / unit (a power of two; a sum of as many as the
+               // vocabulary has fits 62 bits) before their mass is known
+  int list_fine;  // units of a list are so many bits finer (kListUnit, or `unit` if that is finer)
 };
 
 // What a launch does with rows that quick passes do not settle: all of it, or leave them (token
-// kLater), or only what was left.
+// kLater and, where nothing is to be cut, how many bits finer the units that fit the kept mass are),
+// or only what was left.
 enum { kWhole = 0, kQuick = 1, kRest = 2 };
 constexpr int kLater = INT_MIN;
+
+constexpr int kListCap = 2048;  // tokens the first CTA's list holds
+// Bits of a weight of 1 in the units of a whole that fits 62: of all tokens of a vocabulary, of a list.
+constexpr int kMassBits = 61, kListBits = kMassBits - 11;
+constexpr float kListUnit = 1ull << kListBits;
+static_assert(kListCap <= 1 << 11, "the list's mass has to fit 62 bits");
 
 // `clusters` clusters of C CTAs over the rows of q, and what a device needs for that once; one unit
 // of this directory for each logit type and mode.
@@ -80,7 +92,7 @@ namespace {
 constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kPer = 4;              // entries of the first CTA's list a thread takes
-constexpr int kListCap = kPer * kSampleThreads;  // tokens it holds
+static_assert(kListCap == kPer * kSampleThreads, "the list is one round of the CTA");
 constexpr int kResidentMax = 160 * 1024;  // bytes of a row a CTA keeps
 
 
@@ -164,6 +176,10 @@ DS_WEIGHT_FN uint64_t weight_units_of(float m, float c_hi, float c_lo, const flo
 DS_DEV uint64_t weight_units(const WeightMap& w, float l, float unit) {
   return weight_units_of(w.m, w.c_hi, w.c_lo, w.table, l, unit);
 }
+// The exact weight to single precision.
+DS_WEIGHT_FN float weight_of(float m, float c_hi, float c_lo, const float2* table, float l) {
+  return weight_pair(WeightMap{m, c_hi, c_lo, table}, l).x;
+}
 
 // A quick weight is 2^t, t = l c - m c as one fused multiply-add with a rounded m c; what that
 // rounding costs is the same factor for the whole row, known exactly and put back into the sums. A
@@ -246,6 +262,7 @@ struct Shared {
   uint64_t bin[256];
   uint4 edge[2];
   Found found;
+  float4 map;  // m, c_hi, c_lo of the row's map, for put()
 };
 
 constexpr size_t kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
@@ -369,9 +386,10 @@ struct Sampler {
   int C;          // CTAs in the cluster
   uint32_t rank;
   int turn = 0;
-  float m = 0.f, T_r = 1.f, unit;
+  float m = 0.f, T_r = 1.f, unit0;
+  int fine = 0;
   WeightMap map;
-  float c_quick = 0.f, b_quick = 0.f, unit_quick = 0.f;  // log2(e) / T, -m of it, unit and factor
+  float c_quick = 0.f, b_quick = 0.f, fix_quick = 0.f;  // log2(e) / T, -m of it, the row's factor
   bool odd = false;  // the maximum is +inf, or |m| / T past what quick weights take
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -399,9 +417,12 @@ struct Sampler {
     return sh.in[t];
   }
 
-  // Quick weight of l but for the row's factor, which unit_quick has. Not for `odd` rows.
+  // Quick weight of l but for the row's factor, fix_quick. Not for `odd` rows.
   DS_DEV float quick(float l) const { return exp2_approx(fmaf(l, c_quick, b_quick)); }
 
+  // What masses are counted in: units of 1 / unit(), `fine` bits finer than those that fit any row.
+  DS_DEV static float finer(float unit, int bits) { return unit * __int_as_float((127 + bits) << 23); }
+  DS_DEV float unit() const { return finer(unit0, fine); }
   struct Sums {
     uint64_t mass[3];
     uint64_t pre[3];  // of it, in the CTAs before this one
@@ -448,7 +469,7 @@ struct Sampler {
 #pragma unroll
           for (int j = 0; j < J; ++j) n[j] += v[e] > piv[j];
         } else if constexpr (EXACT) {
-          const uint64_t w = weight_units(map, v[e], unit);
+          const uint64_t w = weight_units(map, v[e], unit());
 #pragma unroll
           for (int j = 0; j < J; ++j) x[j] += v[e] > piv[j] ? w : 0;
         } else {
@@ -472,8 +493,9 @@ struct Sampler {
       send_finds();
     }
     if constexpr (MASS && !EXACT) {
+      const float uq = unit() * fix_quick;
 #pragma unroll
-      for (int j = 0; j < J; ++j) x[j] = __float2ull_rn(s[j] * unit_quick);
+      for (int j = 0; j < J; ++j) x[j] = __float2ull_rn(s[j] * uq);
     }
     __syncthreads();  // the sums of the pass before have been read
 #pragma unroll
@@ -501,10 +523,30 @@ struct Sampler {
     }
     if constexpr (!EXACT && MASS) {
       const float mass = __ull2float_rn(r.mass[J - 1]);
-      const float bits = mass > 0.f ? log2f((float)(row.end - row.lead) * unit / mass) : 0.f;
+      const float bits = mass > 0.f ? log2f((float)(row.end - row.lead) * unit() / mass) : 0.f;
       r.err = __float2ull_ru(mass * (kQuickRel + kQuickArg * fmaxf(bits, 0.f)));
     }
     return r;
+  }
+  // Units of 2^-61 to 2^-60 of a quick mass, from units that fit any row; the mass in them.
+  DS_DEV void refine(Sums& z) {
+    const int up = max(0, __clzll((long long)(z.mass[0] + z.err)) - 3);
+    fine += up;
+    z.mass[0] <<= up, z.pre[0] <<= up, z.err <<= up;
+  }
+  // The kept tokens' quick mass, in units that fit any row.
+  DS_DEV Sums quick_mass(const Kept keep) {
+    const float p[3] = {-INFINITY, -INFINITY, -INFINITY};
+    fine = 0;
+    return pass<false, true, 1>(keep, p);
+  }
+  // Units that fit the kept tokens' mass, from exact weights.
+  DS_DEV void exact_units(const Kept keep) {
+    const float p[3] = {-INFINITY, -INFINITY, -INFINITY};
+    fine = 0;
+    Sums z = pass<true, true, 1>(keep, p);
+    z.err = (uint64_t)(row.end - row.lead);
+    refine(z);
   }
 
   // The n-th lowest index (n >= 1) with this logit, among all CTAs.
@@ -606,7 +648,7 @@ struct Sampler {
     int n;
     float high, low;  // the largest logit and the least, but not so low that it weighs nothing
   };
-  DS_DEV void take_list(Entries& t) {
+  DS_DEV void take_list(Entries& t, float unit) {
     t.n = (int)min(sh.n_list, (uint32_t)kListCap);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
@@ -748,13 +790,12 @@ struct Sampler {
     return x;
   }
   // A list of at most one entry a thread, settled by comparing all pairs: its top-k, top-p (of its
-  // own mass, or of `row_mass`, known to within `err`), min-p (all_min_p: the list holds every token
-  // that it keeps) and token. False if `err` leaves the
+  // own mass, or of `row_mass`, in units that fit any row and known to within `err`), min-p (logits
+  // from floor_l up; all_min_p: the list holds all of them) and token. False if `err` leaves the
   // border of top-p open, or the nucleus reaches past the list.
   DS_DEV bool settle_small(const SampleArgs& a, int64_t r, const Entries& t, int k, float top_p,
-                           bool own, uint64_t row_mass, uint64_t err, float min_p, bool all_min_p,
+                           bool own, uint64_t row_mass, uint64_t err, float floor_l, bool all_min_p,
                            float u) {
-    const uint64_t least = min_p > 0.f ? min_p_units(min_p) : 0;
     // each entry is compared by `parts` neighbouring threads
     int parts = 1;
     while (parts < 32 && t.n * parts * 2 <= kSampleThreads) parts *= 2;
@@ -772,13 +813,15 @@ struct Sampler {
       above += __shfl_xor_sync(0xffffffffu, above, o);
       rank_of += __shfl_xor_sync(0xffffffffu, rank_of, o);
     }
+    const bool high = live && key_logit(key) >= floor_l;
     bool in = live && rank_of < (uint32_t)k;
     if (top_p < 1.f) {
-      const uint64_t mine = total(lead && in ? w : 0), basis = own ? mine : row_mass;
-      const uint64_t need = reach_of(top_p, basis), slack = own ? 0 : err + 1;
+      const uint64_t mine = total(lead && in ? w : 0);
+      const uint64_t need = own ? reach_of(top_p, mine) : in_list_units(reach_of(top_p, row_mass), a);
+      const uint64_t slack = own ? 0 : ((err + 1) << a.list_fine) + kListCap;
       if (!own && mine <= need + slack) {
         // the nucleus reaches past the list, but may hold all that min_p keeps
-        const uint64_t some = total(lead && w >= least ? w : 0);
+        const uint64_t some = total(lead && high ? w : 0);
         if (!all_min_p || some + slack > need) return false;
       }
       // the border's entry is the one that reaches `need`
@@ -787,7 +830,7 @@ struct Sampler {
       if (__syncthreads_or(open)) return false;
       in = in && above < need;
     }
-    in = in && w >= least;
+    in = in && high;
     const uint64_t S = total(lead && in ? w : 0), need = past(u, S);  // (all have read sh.extra)
     if (lead && !in) sh.extra[i] = 0;
     __syncthreads();
@@ -795,23 +838,26 @@ struct Sampler {
     for (int j = first; j < t.n; j += parts)
       before += (uint32_t)sh.list[j] > (uint32_t)key ? sh.extra[j] : 0;  // (lower indices)
     for (int o = parts >> 1; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-    if (lead && in && before < need && before + w >= need) put(a, r, key_index(key), w, S);
+    if (lead && in && before < need && before + w >= need) put(a, r, key_index(key), key_logit(key), S, finer(a.unit, a.list_fine));
     return true;
   }
   // The same for a longer list, by bins.
   DS_DEV bool settle_large(const SampleArgs& a, int64_t r, Entries& t, int k, float top_p, bool own,
-                           uint64_t row_mass, uint64_t err, float min_p, bool all_min_p, float u) {
-    const uint64_t least = min_p > 0.f ? min_p_units(min_p) : 0;
+                           uint64_t row_mass, uint64_t err, float floor_l, bool all_min_p, float u) {
+    uint32_t high = 0;  // entries that min-p keeps
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) high |= (uint32_t)(t.key[q] && key_logit(t.key[q]) >= floor_l) << q;
     uint64_t from = 1;  // the least key that stays
     if (t.n > k) from = select<false, false>(t, 1, (uint64_t)k).key;
     if (top_p < 1.f) {
-      const uint64_t mine = list_mass(t, from), basis = own ? mine : row_mass;
-      const uint64_t need = reach_of(top_p, basis), slack = own ? 0 : err + 1;
+      const uint64_t mine = list_mass(t, from);
+      const uint64_t need = own ? reach_of(top_p, mine) : in_list_units(reach_of(top_p, row_mass), a);
+      const uint64_t slack = own ? 0 : ((err + 1) << a.list_fine) + kListCap;
       if (!own && mine <= need + slack) {
         // the nucleus reaches past the list, but may hold all that min_p keeps
         uint64_t some = 0;
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) some += t.w[q] >= least ? t.w[q] : 0;
+        for (int q = 0; q < kPer; ++q) some += high >> q & 1 ? t.w[q] : 0;
         some = total(some);
         if (!all_min_p || some + slack > need) return false;
       } else {
@@ -823,11 +869,15 @@ struct Sampler {
     }
 #pragma unroll
     for (int q = 0; q < kPer; ++q)
-      if (t.w[q] < least) t.w[q] = 0;
+      if (!(high >> q & 1)) t.w[q] = 0;
     const uint64_t S = list_mass(t, from);
     const Found f = select<true, true>(t, from, past(u, S));
-    if (threadIdx.x == 0) put(a, r, key_index(f.key), f.w, S);
+    if (threadIdx.x == 0) put(a, r, key_index(f.key), key_logit(f.key), S, finer(a.unit, a.list_fine));
     return true;
+  }
+  // A mass of the row in units of the list; more than all of a list where it is that.
+  DS_DEV static uint64_t in_list_units(uint64_t x, const SampleArgs& a) {
+    return x >> (62 - a.list_fine) ? 1ull << 62 : x << a.list_fine;
   }
   // The running sum at which a share top_p of a whole is reached: at least 1, at most all of it.
   DS_DEV static uint64_t reach_of(float top_p, uint64_t whole) {
@@ -841,15 +891,13 @@ struct Sampler {
     return u < 1.f ? min(scale_mass(u, S, false) + 1, S) : S;
   }
 
-  // The least weight that min_p keeps, in units.
-  DS_DEV uint64_t min_p_units(float min_p) const { return (uint64_t)(fminf(min_p, 1.f) * unit); }
-  // The lowest logit with at least that weight: 32 candidates at a time (every warp alike).
+  // The lowest logit that weighs at least min_p: 32 candidates at a time (every warp alike).
   DS_DEV float min_p_cut(float min_p) const {
-    const uint64_t least = min_p_units(min_p);
+    const uint64_t least = (uint64_t)(fminf(min_p, 1.f) * kListUnit);
     uint32_t lo = float_key(-INFINITY), hi = float_key(m);  // lo is too low, hi is not
     while (hi - lo > 1) {
       const uint32_t step = max((hi - lo) / 33, 1u), k = min(lo + step * (lane + 1), hi);
-      const uint32_t ok = __ballot_sync(0xffffffffu, weight_units(map, key_logit((uint64_t)k << 32), unit) >= least);
+      const uint32_t ok = __ballot_sync(0xffffffffu, weight_units(map, key_logit((uint64_t)k << 32), kListUnit) >= least);
       const int f = ok ? __ffs(ok) - 1 : 32;
       const uint32_t a = lo + step * f;
       if (f < 32) hi = min(lo + step * (f + 1), hi);
@@ -858,9 +906,13 @@ struct Sampler {
     return key_logit((uint64_t)hi << 32);
   }
 
-  DS_DEV void put(const SampleArgs& a, int64_t r, int token, uint64_t w, uint64_t S) const {
+  // The token, its logit l, and the kept mass S in units of 1 / unit.
+  DS_DEV void put(const SampleArgs& a, int64_t r, int token, float l, uint64_t S, float unit) const {
     a.token[r] = token;
-    if (a.prob) a.prob[r] = __ull2float_rn(w) / __ull2float_rn(S);
+    if (a.prob) {
+      const float4 c = sh.map;
+      a.prob[r] = weight_of(c.x, c.y, c.z, sh.table, l) * unit / __ull2float_rn(S);
+    }
   }
 
   // The first CTA's state and cut to all.
@@ -898,7 +950,7 @@ struct Sampler {
       bool few = false;
       if (g_lo != ~0ull) {
         const uint64_t in = g_lo - g_hi;
-        few = BY_MASS ? (float)kListCap * __ull2float_rn(weight_units(map, v.lo, unit)) >
+        few = BY_MASS ? (float)kListCap * __ull2float_rn(weight_units(map, v.lo, unit())) >
                             1.001f * __ull2float_rn(in + 2 * err)
                       : in <= (uint64_t)kListCap;
       }
@@ -973,7 +1025,7 @@ struct Sampler {
     const uint64_t n_tie = s.n[1] - s.n[0];
     uint64_t n = left;
     if (BY_MASS) {
-      const uint64_t w = weight_units(map, v.hi, unit);
+      const uint64_t w = weight_units(map, v.hi, unit());
       n = w ? (left + w - 1) / w : n_tie;
     }
     if (n >= n_tie) return Kept{v.hi, v.hi == keep.cut ? keep.tie : INT_MAX};
@@ -989,7 +1041,7 @@ struct Sampler {
     Kept cut{v.hi, INT_MAX};
     if (rank == 0) {
       Entries t;
-      take_list(t);
+      take_list(t, unit());
       Found f;
       if (BY_MASS) f = select<false, true>(t, 1, min(left, list_mass(t, 1)));
       else f = select<false, false>(t, 1, left);
@@ -1049,7 +1101,7 @@ struct Sampler {
       const int i0 = row.index(g);
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (l[e] <= v.hi && kept(*cut, l[e], i0 + e)) x += weight_units(map, l[e], unit);
+        if (l[e] <= v.hi && kept(*cut, l[e], i0 + e)) x += weight_units(map, l[e], unit());
     });
     x = warp_sum_u64(x) + w_hi;
     __syncthreads();
@@ -1069,13 +1121,17 @@ struct Sampler {
   }
 
   // The token of a row whose kept set is known, by a pass: quick weights (false: too close to a
-  // border) or exact ones.
+  // border; the units fit the kept mass from then on) or exact ones, in the present units.
   template <bool EXACT>
   DS_DEV bool locate(const SampleArgs& a, int64_t r, const Kept keep, float u) {
     const float p[3] = {-INFINITY, -INFINITY, -INFINITY};
-    const Sums s = keep.cut == -INFINITY ? pass<EXACT, true, 1, true>(keep, p)
-                                         : pass<EXACT, true, 1>(keep, p);
-    return finish<EXACT>(a, r, keep, s.pre[0], s.mass[0], s.err, u);
+    if (!EXACT) fine = 0;
+    Sums s = keep.cut == -INFINITY ? pass<EXACT, true, 1, true>(keep, p) : pass<EXACT, true, 1>(keep, p);
+    // (quick weights are rounded to these units one by one when the token is looked for)
+    if (!EXACT) s.err += (uint64_t)(row.end - row.lead);
+    if (finish<EXACT>(a, r, keep, s.pre[0], s.mass[0], s.err, u)) return true;
+    refine(s);
+    return false;
   }
   // The same from the kept mass S, known to within err, that of the CTAs before this one, and its
   // warps' (sh.wsum[0]).
@@ -1097,10 +1153,11 @@ struct Sampler {
     }
     bool here = false;
     int from = 0, to = 0;
+    const float uq = unit() * fix_quick;
     auto units_of = [&](float l, int i) -> uint64_t {
       if (!(l > -INFINITY) || !kept(keep, l, i)) return 0;
-      if (EXACT) return weight_units(map, l, unit);
-      return __float2ull_rn(quick(l) * unit_quick);
+      if (EXACT) return weight_units(map, l, unit());
+      return __float2ull_rn(quick(l) * uq);
     };
     if (part >= 0) {
       const int f = min(row.g1, row.g0 + part * row.wper), l = min(row.g1, f + row.wper);
@@ -1125,7 +1182,7 @@ struct Sampler {
     int verdict = 0;
     if (here) {
       int token = -1;
-      uint64_t units = 0, cum = before;
+      uint64_t cum = before;
       bool sure = false;
       for (int b = from; b < to; b += 32) {
         float v[E];
@@ -1154,14 +1211,12 @@ struct Sampler {
             for (int e = 0; e < E; ++e) {
               if (token < 0 && c + x[e] >= need) {
                 token = i0 + e;
-                units = x[e];
                 sure = need - c > slack && c + x[e] - need > slack;
               }
               c += x[e];
             }
           }
           token = __shfl_sync(0xffffffffu, token, src);
-          units = __shfl_sync(0xffffffffu, units, src);
           sure = __shfl_sync(0xffffffffu, (int)sure, src) != 0;
           break;
         }
@@ -1169,11 +1224,8 @@ struct Sampler {
       }
       if ((EXACT || sure) && token >= 0) {
         verdict = 1;
-        if (lane == 0) {
-          // (the numerator from the exact weight; S is good to 2^-20)
-          if (!EXACT) units = weight_units(map, to_f32(row.base[row.lead + token]), unit);
-          put(a, r, token, units, S);
-        }
+        // (a quick S is good to 2^-20)
+        if (lane == 0) put(a, r, token, to_f32(row.base[row.lead + token]), S, unit());
       }
     }
     if (EXACT) return true;
@@ -1189,7 +1241,7 @@ struct Sampler {
   DS_DEV void run(const SampleArgs& a, int64_t r, uint4* share, int cluster, uint32_t rk) {
     C = cluster;
     rank = rk;
-    unit = a.unit;
+    unit0 = a.unit;
     const int V = a.vocab;
     const T* start = static_cast<const T*>(a.logits) + r * a.stride;
     row.lead = (int)((reinterpret_cast<uintptr_t>(start) & 15) / sizeof(T));
@@ -1205,6 +1257,8 @@ struct Sampler {
     row.edge = sh.edge;
     row.full0 = row.lead ? 1 : 0;
     row.full1 = row.end / E;
+    // (before the cluster meets: only then is the row's token written)
+    const int left = MODE == kRest ? a.token[r] - kLater : 0;
     if (threadIdx.x < 256) sh.hist[threadIdx.x] = 0;
     if (threadIdx.x == 0) sh.n_list = 0;
     // no CTA writes into another's shared memory before that one runs (waited for below)
@@ -1332,12 +1386,13 @@ struct Sampler {
       return;
     }
     map = weight_map(m, T_r, sh.table);
+    if (threadIdx.x == 0) sh.map = make_float4(map.m, map.c_hi, map.c_lo, 0.f);
     {
       const float mc = m * map.c_hi;
       odd = !(fabsf(mc) < 4194304.f);  // 2^22: the rounding below is 2^-3 at most
       c_quick = fmaxf(map.c_hi, 1e-37f);
       b_quick = -mc;
-      unit_quick = unit * exp2f(-__fmaf_rn(m, map.c_hi, b_quick));
+      fix_quick = exp2f(-__fmaf_rn(m, map.c_hi, b_quick));
     }
     const Kept all{-INFINITY, INT_MAX};
     Kept keep = all;
@@ -1362,15 +1417,15 @@ struct Sampler {
       __syncthreads();  // (announce() clears it)
       if (rank == 0 && found <= (uint32_t)kListCap) {
         Entries t;
-        take_list(t);
+        take_list(t, finer(a.unit, a.list_fine));
         // the mass that top_p is a share of is known exactly if it is the list's: that of its first
         // k tokens, or of the whole row if that is what the list holds
         const bool own = by_k || reach == -INFINITY;
         const int kk = by_k ? k : t.n;
         if (own || !odd) {
           const bool ok = t.n <= kSampleThreads
-                              ? settle_small(a, r, t, kk, top_p, own, z.mass[0], z.err, min_p, all_min_p, u)
-                              : settle_large(a, r, t, kk, top_p, own, z.mass[0], z.err, min_p, all_min_p, u);
+                              ? settle_small(a, r, t, kk, top_p, own, z.mass[0], z.err, floor_l, all_min_p, u)
+                              : settle_large(a, r, t, kk, top_p, own, z.mass[0], z.err, floor_l, all_min_p, u);
           if (ok) state = kDone;
         }
       }
@@ -1380,15 +1435,20 @@ struct Sampler {
     if constexpr (MODE == kQuick) {
       if (floor_l > keep.cut) keep = Kept{floor_l, INT_MAX};
       if (!by_k && !by_p && !odd && locate<false>(a, r, keep, u)) return;
-      if (rank == 0 && threadIdx.x == 0) a.token[r] = kLater;
+      if (rank == 0 && threadIdx.x == 0) a.token[r] = kLater + fine;
       return;
     } else {
       if (by_k) keep = cut_by_number(keep, (uint64_t)k);
       if (by_p) {
-        const float p[3] = {-INFINITY, -INFINITY, -INFINITY};
-        if ((!list || by_k) && !odd) z = pass<false, true, 1>(keep, p);  // (else taken with the list)
+        if (odd) {
+          exact_units(keep);
+        } else {
+          if (!list || by_k) z = quick_mass(keep);  // (else taken with the list)
+          refine(z);
+        }
         bool within = false;  // all that min_p keeps has less than top_p of the mass
         if (floor_l > keep.cut && !odd) {
+          const float p[3] = {-INFINITY, -INFINITY, -INFINITY};
           const Sums s = pass<false, true, 1>(Kept{floor_l, INT_MAX}, p);
           const uint64_t need = reach_of(top_p, z.mass[0]);
           within = s.mass[0] + s.err + z.err + 1 < need;
@@ -1396,8 +1456,10 @@ struct Sampler {
         if (!within && cut_by_mass(a, r, keep, top_p, z, floor_l, u, &keep)) return;
       }
       if (floor_l > keep.cut) keep = Kept{floor_l, INT_MAX};
+      if (odd) exact_units(keep);
       // (a row without a cut was left because quick weights leave its token open)
-      if (!odd && (MODE != kRest || by_k || by_p) && locate<false>(a, r, keep, u)) return;
+      else if (MODE == kRest && !by_k && !by_p) fine = left;
+      else if (locate<false>(a, r, keep, u)) return;
       locate<true>(a, r, keep, u);
     }
   }
@@ -1424,7 +1486,7 @@ __global__ void __launch_bounds__(kSampleThreads, MODE == kQuick ? 2 : 1) k_samp
     const int64_t step = gridDim.x / size;
     for (int64_t r0 = r; r0 < a.rows; r0 += step * kSampleThreads) {
       const int64_t mine = r0 + step * threadIdx.x;
-      const bool is = mine < a.rows && !(a.done && a.done[mine]) && a.token[mine] == kLater;
+      const bool is = mine < a.rows && !(a.done && a.done[mine]) && a.token[mine] <= kLater + kMassBits;
       const uint32_t set = __ballot_sync(0xffffffffu, is);
       __syncthreads();
       if ((threadIdx.x & 31) == 0) left[threadIdx.x >> 5] = set;

@@ -515,9 +515,10 @@ ds_status ds_matmul_fp8(const ds_matmul_fp8_args* args, void* stream);
  * T <= 0 or NaN: the largest logit (lowest index on ties) with prob 1. NaN logits count as -inf;
  * -inf has no mass and is never chosen. A row of nothing but -inf gives token -1, prob 0. u is
  * taken as uniform in [0, 1): below 0 it gives the first token that stays, at 1 and above (and
- * NaN) the last. The token is that of the definition in exact arithmetic up to about 2^-37 of the
- * mass, whatever the layout and the launch; prob is good to 2^-20 (its last bits may depend on the
- * alignment of the row).
+ * NaN) the last. The token is that of the definition in exact arithmetic up to 2^-35 of the mass:
+ * the borders that u S and the filters' shares fall between are each off by no more than that, at
+ * any vocab, layout and launch (weights below 2^-64 of the largest count as none). prob is good to
+ * 2^-20 (its last bits may depend on the alignment of the row).
  *   vocab 1 .. 2^24; temperature, top_k, top_p, min_p [rows], each NULL for 1, 0, 1, 0
  *   u [rows]; done [rows] or NULL: rows with done != 0 are left untouched
  *   token [rows] int32, prob [rows] float or NULL: outputs */

@@ -137,3 +137,115 @@ def test_sampling_with_thousands_of_ties_at_the_kth_logit(dt, R):
                                             top_p=float(np.float32(p)))
             assert margin > 2.0 ** -24 and int(token[r]) == want
             assert abs(float(prob[r]) - pw) <= 2.0 ** -20 * pw
+
+
+def weights(row, T=1.0):
+    """(weights, running sums) of a row in 64 bits and more."""
+    w = np.exp((row - row.max()) / T)
+    return w, np.cumsum(w.astype(np.longdouble))
+
+
+def check_long_row(row, u, token, prob, keep=None):
+    """The token's share of the running sum has u S in it, to 2^-35 of the mass (weights good to 2^-37
+    and rounded to whole units, 2^-37 of the mass in all, in the running sum and in S); prob to 2^-20."""
+    w, _ = weights(row)
+    if keep is not None:
+        w = np.where(keep, w, 0.0)
+    c = np.cumsum(w.astype(np.longdouble))
+    S, goal = c[-1], np.longdouble(np.float32(u)) * c[-1]
+    assert w[token] > 0
+    assert c[token] - w[token] - goal <= 2.0 ** -35 * S and goal - c[token] <= 2.0 ** -35 * S, \
+        (token, float((c[token] - goal) / S))
+    assert abs(prob - float(w[token] / S)) <= 2.0 ** -20 * float(w[token] / S)
+
+
+LONG = 1 << 24
+TAILS = {  # a heavy peak and a long tail of light tokens: where the peak stands, the tail's logit, u's
+    "first": (0, -26.5, (0.5, 0.99993, 0.99997, 0.99999)),
+    "last": (LONG - 1, -26.5, (0.0, 1e-5, 3e-5, 4.7e-5, 0.3)),
+    "lighter": (LONG // 3, -31.0, (1e-8, 2e-7, 0.99, 1.0)),
+    "flat": (LONG // 2, -10.0, (0.01, 0.4, 0.6, 0.97)),
+}
+
+
+@pytest.mark.parametrize("name", TAILS)
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_sampling_keeps_the_mass_of_a_long_light_tail(name, dt):
+    at, tail, us = TAILS[name]
+    logits = torch.full((len(us), LONG), tail, device="cuda").to(DT[dt])
+    logits[:, at] = 0
+    u = torch.tensor(us, device="cuda")
+    row = f64(logits[0])
+    f = lambda v, t=torch.float32: torch.full((len(us),), v, dtype=t, device="cuda")  # noqa: E731
+    order = np.concatenate([[at], np.delete(np.arange(LONG), at)])
+    n = LONG // 2
+    first = np.zeros(LONG, dtype=bool)
+    first[order[:n]] = True
+    for kw, keep in ((dict(), None), (dict(min_p=f(1e-15)), None),
+                     (dict(top_k=f(n, torch.int32)), first)):
+        token, prob = head.sample_logits(logits, u, **kw)
+        for i in range(len(us)):
+            check_long_row(row, us[i], int(token[i]), float(prob[i]), keep)
+    # top_p of the mass, with u at its end: the nucleus ends with the last token that has a part of it
+    w, _ = weights(row)
+    c = np.cumsum(w[order].astype(np.longdouble))
+    for top_p in (0.99995, 0.99999, 0.7):
+        token, prob = head.sample_logits(logits, f(1.0), top_p=f(top_p))
+        need = np.longdouble(np.float32(top_p)) * c[-1]
+        lo, hi = (int(np.searchsorted(c, need + s * 2.0 ** -35 * c[-1])) for s in (-1, 1))
+        last = [int(order[:n + 1].max()) for n in (lo, hi)]
+        assert last[0] <= int(token[0]) <= last[1], (top_p, int(token[0]), last)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_sampling_keeps_the_tail_in_rows_of_many(dt):
+    """The same where each row is one CTA's and some are left to a second launch."""
+    R, V = 160, 1 << 20
+    us = np.linspace(0.0, 2.0 ** -17, R, dtype=np.float32)
+    logits = torch.full((R, V), -26.5, device="cuda").to(DT[dt])
+    logits[:, -1] = 0
+    row = f64(logits[0])
+    token, prob = head.sample_logits(logits, torch.from_numpy(us).cuda())
+    for i in range(0, R, 9):
+        check_long_row(row, us[i], int(token[i]), float(prob[i]))
+
+
+@pytest.mark.parametrize("V", [500, 5003, 65536])
+@pytest.mark.parametrize("T", [0.3, 1.0, 1.7])
+def test_sampling_next_to_a_border(V, T):
+    """u and top_p as near to a border as the definition's answer is still sure, 2^-35 of the mass."""
+    R = 24
+    g = gen(V)
+    logits = 3 * torch.randn(R, V, device="cuda", generator=g)
+    ll = f64(logits)
+    rng = np.random.default_rng(V)
+    cand = (rng.integers(1, 1 << 24, 1 << 20) / 2.0 ** 24).astype(np.float32)
+    u, want, near = np.empty(R, np.float32), [], []
+    p, last = np.empty(R, np.float32), []
+    T32 = float(np.float32(T))
+
+    def closest(c):
+        """The candidate whose share of c[-1] is nearest to a border, and its place."""
+        c = c.astype(np.float64)  # (summed in more)
+        goal = cand.astype(np.float64) * c[-1]
+        i = np.searchsorted(c, goal, side="right")
+        d = np.minimum(np.abs(goal - np.concatenate([[0], c])[i]), np.abs(c[np.minimum(i, len(c) - 1)] - goal))
+        d = np.where(d / c[-1] < 2.0 ** -35, np.inf, d / c[-1])
+        b = int(np.argmin(d))
+        return cand[b], int(i[b]), float(d[b])
+
+    for r in range(R):
+        w, c = weights(ll[r], T32)
+        u[r], at, d = closest(c)
+        want.append(at)
+        near.append(d)
+        order = np.argsort(-ll[r], kind="stable")
+        p[r], at, _ = closest(np.cumsum(w[order].astype(np.longdouble)))
+        last.append(int(order[:at + 1].max()))  # with u = 1: the last of the nucleus
+    assert np.median(near) < 2.0 ** -28 or V == 500
+    t = torch.full((R,), T, device="cuda")
+    token, _ = head.sample_logits(logits, torch.from_numpy(u).cuda(), temperature=t)
+    assert token.tolist() == want
+    token, _ = head.sample_logits(logits, torch.ones(R, device="cuda"), temperature=t,
+                                  top_p=torch.from_numpy(p).cuda())
+    assert token.tolist() == last
