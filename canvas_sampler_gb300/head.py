@@ -253,8 +253,10 @@ def head_status(device=None, stream=None) -> int:
 class OutputHead:
     """A final norm and a vocabulary table held in 8 bits, from hidden states to tokens.
 
-    E [V, d] (bf16 or fp32, on the device) is quantised once, in 128 x 128 blocks; norm_weight [d]
-    has the hidden states' type. Calls share nothing but these read-only weights.
+    E [V, d] (bf16 or fp32, on the device) is quantised once, in 128 x 128 blocks, on the current
+    stream; norm_weight [d] has the hidden states' type. The constructor returns when the table is
+    ready (unless it is being captured into a graph), so calls on any stream may follow it. Calls share
+    nothing but these read-only weights.
     """
 
     def __init__(self, E: torch.Tensor, norm_weight: torch.Tensor, *, eps: float = 1e-6,
@@ -262,10 +264,13 @@ class OutputHead:
         self.vocab, self.d = _shape("E", E)
         if norm_weight is None:
             raise ValueError("norm_weight is required")
-        self.q, self.scales = quantize_fp8(E, fp8=fp8)
-        _vector("norm_weight", norm_weight, self.d, norm_weight.dtype, E.get_device())
         if out_dtype not in _OUT:
             raise ValueError(f"out_dtype must be one of {sorted(_OUT)}")
+        _vector("norm_weight", norm_weight, self.d, norm_weight.dtype, E.get_device())
+        self.q, self.scales = quantize_fp8(E, fp8=fp8)
+        with torch.cuda.device(E.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
         self.norm_weight, self.eps, self.weight_offset = norm_weight, eps, weight_offset
         self.fp8, self.out_dtype = fp8, out_dtype
 

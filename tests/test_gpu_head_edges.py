@@ -249,3 +249,38 @@ def test_sampling_next_to_a_border(V, T):
     token, _ = head.sample_logits(logits, torch.ones(R, device="cuda"), temperature=t,
                                   top_p=torch.from_numpy(p).cuda())
     assert token.tolist() == last
+
+
+# ------------------------------------------------------------------------------------- together
+def test_first_use_of_a_head_on_another_stream():
+    """A call on any stream right after the constructor sees the whole table."""
+    V, d, R = 131072, 1024, 16
+    g = gen(41)
+    w = torch.ones(d, device="cuda").bfloat16()
+    x = torch.randn(R, d, device="cuda", generator=g).bfloat16()
+    u = torch.rand(R, device="cuda", generator=g)
+    side = torch.cuda.Stream()
+    for seed in range(4):
+        E = torch.randn(V, d, device="cuda", generator=gen(seed)).bfloat16()
+        torch.cuda.synchronize()
+        hd = head.OutputHead(E, w, out_dtype="fp32")
+        first, _ = hd.logits(x, stream=side)
+        token, _ = hd.sample(x, u, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(hd.logits(x)[0], first) and torch.equal(hd.sample(x, u)[0], token)
+
+
+def test_a_head_built_inside_a_capture():
+    V, d, R = 3000, 256, 5
+    g = gen(42)
+    E = torch.randn(V, d, device="cuda", generator=g).bfloat16()
+    w = torch.ones(d, device="cuda").bfloat16()
+    x = torch.randn(R, d, device="cuda", generator=g).bfloat16()
+    want, _ = head.OutputHead(E, w, out_dtype="fp32").logits(x)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out, _ = head.OutputHead(E, w, out_dtype="fp32").logits(x)
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
