@@ -16,8 +16,13 @@ namespace {
 
 using namespace tcpipe;
 
-// Error bits of this device's products (kErrTimeout), read and cleared by ds_head_status.
-__device__ uint32_t g_matmul_fp8_err = 0;
+// Error bits of this device's products (kErrTimeout), and those that ds_head_status took from it last:
+// one exchange reads and clears, so that a bit set by a product on another stream meanwhile is not lost.
+__device__ uint32_t g_matmul_fp8_err = 0, g_matmul_fp8_taken = 0;
+__global__ void k_take_matmul_fp8_errors() {
+  pdl_wait();
+  g_matmul_fp8_taken = atomicExch(&g_matmul_fp8_err, 0u);
+}
 
 // ------------------------------------------------------------------------------------------
 // CUDA cores: any strides and bases
@@ -611,14 +616,12 @@ cudaError_t launch_matmul_fp8_tc(const ds_matmul_fp8_args& a, cudaStream_t st) {
 }
 
 cudaError_t read_matmul_fp8_errors(uint32_t* word, cudaStream_t st) {
-  const uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_matmul_fp8_err, sizeof(*word), 0,
-                                            cudaMemcpyDeviceToHost, st);
+  static std::mutex m;  // one reader at a time has g_matmul_fp8_taken
+  std::lock_guard<std::mutex> lock(m);
+  cudaError_t e = launch_k(k_take_matmul_fp8_errors, dim3(1), dim3(1), 0, st);
+  if (e == cudaSuccess)
+    e = cudaMemcpyFromSymbolAsync(word, g_matmul_fp8_taken, sizeof(*word), 0, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  if (e == cudaSuccess && *word) {
-    e = cudaMemcpyToSymbolAsync(g_matmul_fp8_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  }
   return e;
 }
 

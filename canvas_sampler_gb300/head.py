@@ -239,7 +239,8 @@ def sample_logits(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.T
 
 
 def head_status(device=None, stream=None) -> int:
-    """ds_head_status of a device (the current one by default): 0, or a DS_ERR_* code."""
+    """ds_head_status of a device (the current one by default): 0, or a DS_ERR_* code. Its error word
+    is shared by all callers and streams of the device, and taken by this call."""
     v = c_int32()
     dev = torch.cuda.current_device() if device is None else torch.device(device).index
 

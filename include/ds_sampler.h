@@ -406,8 +406,9 @@ ds_status ds_sampler_debug_buffer(ds_sampler* sampler, int32_t which, const void
  * mode -- report section 6, "Sampling" -- but gives neither the formats nor the filters; those
  * here are the plain definitions stated with each entry point.)
  *
- * These calls need no sampler, allocate nothing, keep nothing between calls and use no shared
- * workspace: any number may run at once, on any streams, and be captured into graphs. All
+ * These calls need no sampler, allocate nothing and use no shared workspace; all they keep between
+ * calls is one error word a device (ds_head_status). Any number may run at once, on any streams,
+ * and be captured into graphs. All
  * pointers are [device], on the device that is current at the call. Strides count elements from
  * one row to the next; rows may be longer than what is used of them. Rows past the end of an
  * argument and columns past its width are never read or written. A call with no rows returns
@@ -540,9 +541,11 @@ typedef struct ds_sample_logits_args {
 } ds_sample_logits_args;
 ds_status ds_sample_logits(const ds_sample_logits_args* args, void* stream);
 
-/* Device status of the 8-bit head's products on the current device since the last call:
- * synchronises `stream`, reads the error word and clears it. *out = DS_OK or DS_ERR_TIMEOUT (a
- * bounded wait ran out; outputs since then are not valid). Not for use inside stream capture. */
+/* Device status of the 8-bit head's products on the current device since the last call, by whomever:
+ * all callers and streams of a device share one error word. Takes the word (reads and clears it in
+ * one step) in the order of `stream` and synchronises it. *out = DS_OK or DS_ERR_TIMEOUT (a bounded
+ * wait ran out in some product since the last call; outputs since then are not valid). Not for use
+ * inside stream capture. */
 ds_status ds_head_status(void* stream, ds_status* out);
 
 #ifdef __cplusplus

@@ -284,3 +284,27 @@ def test_a_head_built_inside_a_capture():
     gr.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_status_calls_beside_products_on_other_streams():
+    """Two threads take the error word while products run on their streams."""
+    import threading
+    ops = operands(300, 5000, 384, 7)
+    want = head.matmul_fp8(*ops, out_dtype="fp32")
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        for _ in range(40):
+            got = head.matmul_fp8(*ops, out_dtype="fp32", stream=s)
+            st = head.head_status(stream=s)  # (synchronises s)
+            if st != 0 or not torch.equal(got, want):
+                bad.append(st)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
