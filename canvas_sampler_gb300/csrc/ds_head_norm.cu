@@ -33,11 +33,12 @@ struct Raw8 {
   uint32_t w[2 * sizeof(T)];
 };
 
-// Columns c .. c + 7 of a row of n (zeros past its end); VEC: the row is 16-byte aligned.
+// Columns c .. c + 7 of a row of n (zeros past its end); VEC: the row is 16-byte aligned. (At the end
+// of the longest row c + 8 passes 2^31; n - c and n - 8 stay below.)
 template <typename T, bool VEC>
 DS_DEV Raw8<T> load8(const T* row, int c, int n) {
   Raw8<T> t;
-  if (VEC && c + 8 <= n) {
+  if (VEC && c <= n - 8) {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
       const uint4 q = reinterpret_cast<const uint4*>(row + c)[i];
@@ -47,10 +48,10 @@ DS_DEV Raw8<T> load8(const T* row, int c, int n) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if constexpr (sizeof(T) == 4) {
-        t.w[i] = c + i < n ? __float_as_uint(row[c + i]) : 0u;
+        t.w[i] = i < n - c ? __float_as_uint(row[c + i]) : 0u;
       } else {
         const uint32_t v =
-            c + i < n ? (uint32_t)reinterpret_cast<const unsigned short*>(row)[c + i] : 0u;
+            i < n - c ? (uint32_t)reinterpret_cast<const unsigned short*>(row)[c + i] : 0u;
         t.w[i >> 1] = i & 1 ? t.w[i >> 1] | v << 16 : v;
       }
     }
@@ -60,7 +61,7 @@ DS_DEV Raw8<T> load8(const T* row, int c, int n) {
 
 template <typename T, bool VEC>
 DS_DEV void store8(T* row, int c, int n, const Raw8<T>& t) {
-  if (VEC && c + 8 <= n) {
+  if (VEC && c <= n - 8) {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i)
       reinterpret_cast<uint4*>(row + c)[i] =
@@ -68,7 +69,7 @@ DS_DEV void store8(T* row, int c, int n, const Raw8<T>& t) {
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + i < n) {
+      if (i < n - c) {
         if constexpr (sizeof(T) == 4) row[c + i] = __uint_as_float(t.w[i]);
         else reinterpret_cast<unsigned short*>(row)[c + i] = (unsigned short)(t.w[i >> 1] >> (16 * (i & 1)));
       }
@@ -141,12 +142,12 @@ DS_DEV void store_codes(uint8_t* row, int c, int n, const float (&y)[8], const F
     p[i] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, kind);
   }
   const uint32_t w[2] = {p[0] | (p[1] << 16), p[2] | (p[3] << 16)};
-  if (VEC && c + 8 <= n) {
+  if (VEC && c <= n - 8) {
     *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + i < n) row[c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+      if (i < n - c) row[c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
   }
 }
 

@@ -1,9 +1,12 @@
 """The 8-bit output head where it can go wrong: values halfway between two codes, products of several
 tiles a CTA."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
+from canvas_sampler_gb300 import _lib as C
 from canvas_sampler_gb300 import head
 from oracle import head as O
 
@@ -308,3 +311,28 @@ def test_status_calls_beside_products_on_other_streams():
     for t in threads:
         t.join()
     assert not bad
+
+
+# ------------------------------------------------------------------------------------- long rows
+def test_quantising_the_longest_row():
+    """2^31 - 1 columns: the last group of eight has seven, and nothing beside them is read or written."""
+    n = 2 ** 31 - 1
+    x = torch.zeros(n + 9, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(300, device="cuda", generator=gen(3)).bfloat16()
+    x[n - 300:n] = tail
+    x[n:] = 1e30
+    q = torch.full((n + 17,), 77, dtype=torch.uint8, device="cuda")
+    s = torch.full((n // 128 + 2,), -1.0, device="cuda")
+    args = C.ds_quantize_fp8_args(rows=1, cols=n, dtype=C.DS_DTYPE_BF16, fp8=C.DS_FP8_E4M3, block_rows=1,
+                                  x=x.data_ptr(), x_stride=n + 1, q=q.data_ptr(), q_stride=n + 1,
+                                  scales=s.data_ptr(), scales_stride=n // 128 + 1)
+    C.check(C.load_library().ds_quantize_fp8(ctypes.byref(args), torch.cuda.current_stream().cuda_stream),
+            "ds_quantize_fp8")
+    torch.cuda.synchronize()
+    assert torch.all(q[n:] == 77) and float(s[-1]) == -1.0
+    at = n // 128 * 128  # the last block: 127 columns
+    y = f64(tail[-(n - at):])[None, :]
+    v = quotients(y, "e4m3", 1)
+    assert np.array_equal(f64(q[at:n].view(torch.float8_e4m3fn))[None, :], O.fp8_round(v.astype(np.float32), "e4m3"))
+    assert abs(float(s[-2]) - np.abs(y).max() / 448) <= 2.0 ** -24 * np.abs(y).max() / 448
+    assert int(q[:n - 500].max()) == 0
