@@ -94,7 +94,12 @@ def _elsewhere(dev: int, stream):
 
 
 def _run(work, dev: int, stream):
-    """work(raw stream) where the tensors live."""
+    """work(raw stream) where the tensors live. A stream object has to be of their device (of a bare
+    handle only the caller knows that)."""
+    if stream is not None:
+        on = getattr(stream, "device", None)
+        if on is not None and on.index != dev:
+            raise ValueError(f"stream: expected one of cuda:{dev}, got one of {on}")
     if stream is None and _current_device() == dev:  # (a tensor is on it: CUDA is up)
         return work(_raw_stream(dev))
     with _elsewhere(dev, stream) as raw:
