@@ -8,7 +8,8 @@ one of the library's CUDA kernels. The four operators stand alone; OutputHead ru
     token, prob = head.sample(x, u, residual, top_p=p)       # and a token per row
 
 A call enqueues its work on `stream` (the current stream of the tensors' device by default),
-allocates its outputs there and shares no workspace with any other call.
+allocates its outputs there and shares no workspace with any other call. There is no backward pass:
+tensors that require a gradient are refused unless gradients are off (torch.no_grad()).
 """
 from __future__ import annotations
 
@@ -40,9 +41,18 @@ def _entry(name: str):
     return C.packed_call(name, getattr(C, name + "_args"))
 
 
+def _refuse_gradient(name: str) -> None:
+    """These operators have no backward pass: outputs would leave the graph without a word."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name} wants a gradient, which these operators do not give: call them "
+                         "under torch.no_grad() or with detached tensors")
+
+
 def _rows(name: str, t, shape: tuple, dtypes, dev: int) -> int:
     """Check a [rows, columns] argument whose columns are adjacent; the elements from one row to
     the next. A lone row has no next one: any stride that keeps its start's alignment serves."""
+    if isinstance(t, torch.Tensor) and t.requires_grad:
+        _refuse_gradient(name)
     if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and \
             t.get_device() == dev and dev >= 0:
         s = t.stride()
@@ -68,6 +78,8 @@ def _vector(name: str, t, n: int, dtype, dev: int) -> int:
     """Check an [n] argument; its address, 0 for None."""
     if t is None:
         return 0
+    if isinstance(t, torch.Tensor) and t.requires_grad:
+        _refuse_gradient(name)
     if isinstance(t, torch.Tensor) and t.shape == (n,) and t.dtype is dtype and \
             t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
@@ -260,7 +272,8 @@ class OutputHead:
     """A final norm and a vocabulary table held in 8 bits, from hidden states to tokens.
 
     E [V, d] (bf16 or fp32, on the device) is quantised once, in 128 x 128 blocks, on the current
-    stream; norm_weight [d] has the hidden states' type. The constructor returns when the table is
+    stream; norm_weight [d] has the hidden states' type. Both are constants here: parameters are taken
+    without their gradients. The constructor returns when the table is
     ready (unless it is being captured into a graph), so calls on any stream may follow it. Calls share
     nothing but these read-only weights.
     """
@@ -270,6 +283,7 @@ class OutputHead:
         self.vocab, self.d = _shape("E", E)
         if norm_weight is None:
             raise ValueError("norm_weight is required")
+        E, norm_weight = E.detach(), norm_weight.detach()
         if out_dtype not in _OUT:
             raise ValueError(f"out_dtype must be one of {sorted(_OUT)}")
         _vector("norm_weight", norm_weight, self.d, norm_weight.dtype, E.get_device())

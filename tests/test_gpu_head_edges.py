@@ -336,3 +336,26 @@ def test_quantising_the_longest_row():
     assert np.array_equal(f64(q[at:n].view(torch.float8_e4m3fn))[None, :], O.fp8_round(v.astype(np.float32), "e4m3"))
     assert abs(float(s[-2]) - np.abs(y).max() / 448) <= 2.0 ** -24 * np.abs(y).max() / 448
     assert int(q[:n - 500].max()) == 0
+
+
+# ------------------------------------------------------------------------------------- gradients
+def test_inputs_that_want_a_gradient():
+    """Refused by the operators while gradients are on; constants to a head, as its own weights."""
+    g = gen(51)
+    E = torch.nn.Parameter(torch.randn(1000, 256, device="cuda", generator=g).bfloat16())
+    w = torch.nn.Parameter(torch.ones(256, device="cuda").bfloat16())
+    x = torch.randn(3, 256, device="cuda", generator=g).bfloat16()
+    u = torch.rand(3, device="cuda", generator=g)
+    hd = head.OutputHead(E, w)
+    logits, _ = hd.logits(x)
+    leaf = x.clone().requires_grad_()
+    for call in (lambda: head.rmsnorm_fp8(x, w), lambda: head.rmsnorm_fp8(leaf, w.detach()),
+                 lambda: head.rmsnorm_fp8(x, w.detach(), leaf), lambda: head.quantize_fp8(E),
+                 lambda: hd.sample(leaf, u), lambda: head.sample_logits(logits.float().requires_grad_(), u)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    with torch.no_grad():
+        got, _ = hd.logits(leaf)
+        q, _ = head.quantize_fp8(E)
+    assert torch.equal(got, logits) and torch.equal(q.view(torch.uint8), hd.q.view(torch.uint8))
+    assert not got.requires_grad and not logits.requires_grad
