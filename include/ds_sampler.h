@@ -425,8 +425,11 @@ enum { DS_FP8_E4M3 = 0, DS_FP8_E5M2 = 1 };
  *   for each 128 columns: scale = max(max |y|, 2^-100) / F, q = y / scale rounded to fp32 and then to
  *   the nearest code (ties to even), saturating. The codes see no other rounding than this and that
  *   of h * (weight_offset + weight) to fp32; a scale is good to 2^-18.
- * Sums and products are fp32 (so |h| above 1.8e19 overflows the mean). A NaN in y becomes a NaN
- * code and does not enter the scale.
+ * Sums and products are fp32: |h| above 1.8e19 overflows the mean (y = 0 then), and squares of |h|
+ * below 2^-63 lose bits, below 2^-75 all of them, which shows only where eps does not cover them
+ * (with eps = 0, a row of such values is divided by 0, and so is a row of zeros). A NaN in y becomes a
+ * NaN code and does not enter the scale; a block whose largest |y| is infinite has an infinite scale,
+ * NaN codes for its infinite values and 0 for the others.
  *   rows, d         [rows, d]; 0 <= rows <= 2^30, 1 <= d <= 32768 (else DS_ERR_UNSUPPORTED)
  *   dtype           type of x, residual, weight and h (DS_DTYPE_*); fp8: DS_FP8_*
  *   x, residual     inputs; residual may be NULL

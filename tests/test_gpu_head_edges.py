@@ -359,3 +359,34 @@ def test_inputs_that_want_a_gradient():
         q, _ = head.quantize_fp8(E)
     assert torch.equal(got, logits) and torch.equal(q.view(torch.uint8), hd.q.view(torch.uint8))
     assert not got.requires_grad and not logits.requires_grad
+
+
+# ------------------------------------------------------------------------------------- special rows
+def test_norm_of_each_special_row():
+    """With eps = 0: zeros are 0 / 0; squares below fp32's least (|h| below 2^-75) sum to 0, and h / 0
+    is infinite; small rows whose squares fp32 holds are rows like others; NaN and infinities."""
+    nan, inf = float("nan"), float("inf")
+    x = torch.zeros(7, 256, device="cuda")
+    x[1, 3] = nan
+    x[2] = 1e-30
+    x[3] = 1e-18
+    x[4, 7], x[4, 200] = inf, 1.0
+    x[5, 5] = 1e19
+    x[6, 0], x[6, 255] = 2e19, 1.0  # (4e38: the sum overflows)
+    w = torch.ones(256, device="cuda")
+    q, s, h = head.rmsnorm_fp8(x, w, eps=0.0)
+    q, s = f64(q), f64(s)
+    tiny = float(np.float32(O.TINY / 448))
+    assert h is x
+    for r in (0, 1):  # y is NaN throughout, and NaN does not enter a scale
+        assert np.isnan(q[r]).all() and (s[r] == tiny).all(), r
+    assert np.isnan(q[2]).all() and np.isinf(s[2]).all()
+    assert (q[3] == 448).all() and np.allclose(s[3], 1 / 448, rtol=2.0 ** -18, atol=0)
+    assert np.isnan(q[4, 7]) and (np.delete(q[4], 7) == 0).all() and (s[4] == tiny).all()
+    want = np.zeros(256)
+    want[5] = 448
+    assert (q[5] == want).all()
+    assert np.allclose(s[5], [16 / 448, tiny], rtol=2.0 ** -18, atol=0)
+    assert (q[6] == 0).all() and (s[6] == tiny).all()
+    q, s, _ = head.rmsnorm_fp8(x[2:3], w, eps=1e-6)  # eps covers it: y = 1e-27, above 2^-100
+    assert (f64(q) == 448).all() and np.allclose(f64(s), 1e-27 / 448, rtol=2.0 ** -18, atol=0)
