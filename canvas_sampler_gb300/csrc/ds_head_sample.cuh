@@ -125,11 +125,12 @@ DS_DEV WeightMap weight_map(float m, float T, const float2* table) {
   return WeightMap{m, c, c >= 3e38f || c == 0.f ? 0.f : rest / T, table};
 }
 
-// e^((l - m) / T) as a float pair, for l <= m; relative error about 2^-37. l - m and its product
-// with the factor are kept with their rounding errors (two-sum, fused multiply-add); 2^t splits
-// into a power of two, a table entry and e^z with |z| < 0.011, whose series stops at z^5 / 120
-// (the next term is below 2^-48) and is below 2^-14 from its second-order term on, so that part
-// needs single precision only.
+// e^((l - m) / T) as a float pair, for l <= m; relative error about 2^-37. The table-driven method of
+// P. T. P. Tang (ACM Transactions on Mathematical Software 15, 1989) in pairs of floats: sums with
+// their rounding errors by Knuth's two-sum and, where the larger term is known, Dekker's; products
+// with theirs by a fused multiply-add. 2^t splits into a power of two, a table entry and e^z with
+// |z| < 0.011, whose series stops at z^5 / 120 (the next term is below 2^-48) and is below 2^-14 from
+// its second-order term on, so that part needs single precision only.
 DS_DEV float2 weight_pair(const WeightMap& w, float l) {
   const float d = __fsub_rn(l, w.m);
   const float t0 = __fmul_rn(d, w.c_hi), t = fmaxf(t0, -64.f);
@@ -481,7 +482,7 @@ struct Sampler {
       }
       if constexpr (MASS && !EXACT) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {  // compensated running sum
+        for (int j = 0; j < J; ++j) {  // running sum, compensated as by W. Kahan (1965)
           const float y = part[j] - comp[j], z = s[j] + y;
           comp[j] = (z - s[j]) - y;
           s[j] = z;

@@ -390,3 +390,54 @@ def test_norm_of_each_special_row():
     assert (q[6] == 0).all() and (s[6] == tiny).all()
     q, s, _ = head.rmsnorm_fp8(x[2:3], w, eps=1e-6)  # eps covers it: y = 1e-27, above 2^-100
     assert (f64(q) == 448).all() and np.allclose(f64(s), 1e-27 / 448, rtol=2.0 ** -18, atol=0)
+
+
+# ------------------------------------------------------------------------------------- no row excused
+def away_from_borders(logits, u, kw):
+    """u and top_p moved until every row's answer is sure (borders 2^-34 of the mass away): all rows
+    can be compared. Returns the expected (token, prob) of each."""
+    ll, want = f64(logits), []
+    v = {n: t.cpu().numpy() for n, t in kw.items()}
+    uu = u.cpu().numpy()
+    for r in range(len(ll)):
+        for _ in range(30):
+            row = {("T" if n == "temperature" else n): t[r].item() for n, t in v.items()}
+            token, prob, margin = O.sample_row(ll[r], float(uu[r]), **row)
+            if margin >= 2.0 ** -34:
+                break
+            uu[r] = np.float32((uu[r] + 0.0371) % 1.0)
+            if 0 < v["top_p"][r] < 1:
+                v["top_p"][r] = np.float32(v["top_p"][r] * 0.9967)
+        else:
+            raise AssertionError(f"row {r} stays next to a border")
+        want.append((token, prob))
+    return torch.from_numpy(uu).cuda(), {n: torch.from_numpy(t).cuda() for n, t in v.items()}, want
+
+
+def rows_of(R, V, seed, kind):
+    g = gen(seed)
+    if kind == "normal":
+        return torch.randn(R, V, device="cuda", generator=g)
+    if kind == "steep":
+        return 2.0 * -torch.log(torch.rand(R, V, device="cuda", generator=g).clamp(min=1e-9)) - 10
+    if kind == "ties":
+        return (4 * torch.randn(R, V, device="cuda", generator=g)).round() / 2
+    return torch.full((R, V), 0.5, device="cuda")
+
+
+@pytest.mark.parametrize("R,V", [(400, 5003), (330, 16001), (160, 40009), (24, 262144), (3, 700001)])
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_sampling_of_every_row(R, V, dt):
+    kinds = [rows_of(-(-R // 4), V, R + i, k) for i, k in enumerate(("normal", "steep", "ties", "flat"))]
+    logits = torch.stack(kinds, dim=1).view(-1, V)[:R].contiguous().to(DT[dt])
+    pick = lambda *v: torch.tensor([v[(i // 4 + i) % len(v)] for i in range(R)], device="cuda")  # noqa: E731
+    kw = dict(temperature=pick(1.0, 0.7, 1.0, 1.3, 0.0, 0.9, 2.0),
+              top_k=pick(0, 40, 0, 3000, 0, 0, 1, 0, 0, 0, 700).int(),
+              top_p=pick(1.0, 0.9, 0.95, 0.6, 0.9, 1.0, 0.999, 0.8, 0.5),
+              min_p=pick(0.0, 0.0, 0.05, 0.0, 0.0, 0.001, 0.0, 0.0))
+    u = torch.rand(R, device="cuda", generator=gen(R))
+    u, kw, want = away_from_borders(logits, u, kw)
+    token, prob = head.sample_logits(logits, u, **kw)
+    assert token.tolist() == [t for t, _ in want]
+    p = np.array([p for _, p in want])
+    assert np.all(np.abs(f64(prob) - p) <= 2.0 ** -20 * p)
