@@ -187,7 +187,9 @@ DS_WEIGHT_FN float weight_of(float m, float c_hi, float c_lo, const float2* tabl
 // mass of quick weights is then off by no more than mass 2^-20 (the special-function unit's own 2^-22
 // and the fp32 additions of a thread's sum, compensated: a few 2^-24) and sum w |t| 2 2^-24 ln 2 (the
 // roundings of t and of c); and sum w |t| is no more than mass log2(n / mass) for n tokens with the
-// largest weight 1, since the entropy of n tokens is no more than log2 n.
+// largest weight 1, since the entropy of n tokens is no more than log2 n. prob is a weight over such a
+// mass where the token needed no other: that is its 2^-20, and why its last bits follow the row's
+// alignment. Exact masses everywhere would take 708 us where these take 102 (256 x 262144 bf16).
 constexpr float kQuickRel = 9.6e-7f, kQuickArg = 1e-7f;
 
 // ceil(x whole) and floor(x whole) for x in (0, 1): 64-bit floats cost this machine more than the

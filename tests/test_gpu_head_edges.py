@@ -441,3 +441,72 @@ def test_sampling_of_every_row(R, V, dt):
     assert token.tolist() == [t for t, _ in want]
     p = np.array([p for _, p in want])
     assert np.all(np.abs(f64(prob) - p) <= 2.0 ** -20 * p)
+
+
+# ------------------------------------------------------------------------------------- captures
+def test_the_first_calls_of_a_process_inside_a_capture():
+    """What the library sets up once a device may be set up while a stream is being captured."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from canvas_sampler_gb300 import head
+g = torch.Generator(device="cuda"); g.manual_seed(1)
+x = torch.randn(400, 512, device="cuda", generator=g).bfloat16()
+E = torch.randn(6000, 512, device="cuda", generator=g).bfloat16()
+w = torch.ones(512, device="cuda").bfloat16()
+u = torch.rand(400, device="cuda", generator=g)
+p = torch.full((400,), 0.97, device="cuda")
+def run():
+    q, s = head.quantize_fp8(E)
+    a, sa, _ = head.rmsnorm_fp8(x, w)
+    y = head.matmul_fp8(a, sa, q, s, out_dtype="fp32")
+    few = head.matmul_fp8(a[:3], sa[:3], q, s)
+    return y, few, *head.sample_logits(y, u, top_p=p), *head.sample_logits(few, u[:3], top_p=p[:3])
+torch.cuda.synchronize()
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    out = run()
+gr.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in out]
+want = run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert head.head_status() == 0
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_graphs_replayed_at_once():
+    """Two captured calls on two streams share nothing but the weights."""
+    g = gen(61)
+    E = torch.randn(20000, 256, device="cuda", generator=g).bfloat16()
+    hd = head.OutputHead(E, torch.ones(256, device="cuda").bfloat16())
+    R = 400
+    sets = [torch.randn(R, 256, device="cuda", generator=g).bfloat16() for _ in range(2)]
+    u = torch.rand(R, device="cuda", generator=g)
+    kw = dict(top_p=torch.full((R,), 0.97, device="cuda"),
+              top_k=(torch.arange(R, device="cuda") % 3 * 1000).int())
+    want = [hd.sample(x, u, **kw) for x in sets]
+    torch.cuda.synchronize()
+    graphs = []
+    for x in sets:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = hd.sample(x, u, **kw)
+        graphs.append((gr, out, torch.cuda.Stream()))
+    for _ in range(10):
+        for _, out, _ in graphs:
+            out[0].fill_(-5)
+        torch.cuda.synchronize()
+        for gr, _, s in graphs:
+            with torch.cuda.stream(s):
+                gr.replay()
+        torch.cuda.synchronize()
+        for (_, out, _), w in zip(graphs, want):
+            assert torch.equal(out[0], w[0]) and torch.equal(out[1], w[1])
