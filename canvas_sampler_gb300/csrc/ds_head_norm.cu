@@ -12,9 +12,9 @@
 // either (only that of h (offset + w)). The floor of 2^-100 keeps s and 1/s finite for blocks of zeros.
 //
 // Both kernels touch each byte once. The table's quantisation is bound by memory (262144 x 2816 bf16:
-// 324 us, 6.8 TB/s). The norm is too where a row is a warp's (65536 x 256 fp32: 36 us, 6.1 TB/s);
+// 322 us, 6.9 TB/s). The norm is too where a row is a warp's (65536 x 256 fp32: 36 us, 6.1 TB/s);
 // longer rows pay for the sum across warps and about 30 instructions a value (65536 x 2816 bf16 with
-// a residual: 257 us, 5.0 TB/s; 16001 x 5000: 121 us, 4.6 TB/s; one row: 2.3 us).
+// a residual: 256 us, 5.0 TB/s; 16001 x 5000: 117 us, 4.8 TB/s; one row: 2.4 us).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -293,8 +293,9 @@ DS_DEV float amax8(const Raw8<T>& t) {
 }
 
 // One 128 x 128 block a CTA of 256 threads: 16 threads across, 16 rows at a time, 8 loads of 8
-// columns in flight a thread, four CTAs an SM for bf16 (262144 x 2816: 324 us; three, 354). ROWS: each row of the block has its own scale. Blocks go to CTAs
-// along the rows of x, so that the CTAs that run together read whole rows.
+// columns in flight a thread, four CTAs an SM for bf16 (262144 x 2816: 324 us; three, 354). ROWS:
+// each row of the block has its own scale. Blocks go to CTAs along the rows of x, so that the CTAs
+// that run together read whole rows.
 template <typename T, bool VEC, bool ROWS, bool E5M2>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) k_quantize_fp8(const QuantArgs a) {
   __shared__ float part[8];
@@ -380,7 +381,7 @@ cudaError_t launch_rmsnorm_fp8(const ds_rmsnorm_fp8_args& a, cudaStream_t st) {
   // Groups of 8 columns a thread: one, unless a row then takes 513 to 768 threads, of which an SM
   // holds one row only (at 64 registers a thread): two then, and two rows (at 80). Measured, bf16
   // with a residual, one group: 65536 x 2816 257 us, 16384 x 8192 169 us, 16001 x 5000 187 us; two:
-  // 16001 x 5000 121 us (one row an SM, 128 registers: 140). More where a row has more than 8192
+  // 16001 x 5000 117 us (one row an SM, 128 registers: 140). More where a row has more than 8192
   // columns.
   int nv = groups > 512 && groups <= 768 ? 2 : 1;
   if (groups > 1024)

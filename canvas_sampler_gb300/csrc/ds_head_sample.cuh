@@ -32,8 +32,8 @@
 // are marked and taken by larger clusters in a second launch (ds_head_sample.cu).
 //
 // Bound: the floor is one read of the logits, 20 us at 256 x 262144 bf16 and 40 us at 2048 x 32749
-// fp32; the first launches there take 55 (top-k and top-p) to 86 us (nucleus) and 97 (token by mass)
-// to 130 us. At the first size two reads from memory are 40 us of it; beyond that it is issue slots
+// fp32; the first launches there take 56 (top-k and top-p) to 86 us (nucleus) and 97 (token by mass)
+// to 143 us (nucleus). At the first size two reads from memory are 40 us of it; beyond that it is issue slots
 // (26 instructions a token) and a row's last steps, over a list of some tens to two thousand tokens,
 // which keep a CTA waiting on barriers and shuffles. 64-bit floats cost thousands of cycles a row here
 // and are not used. One row over eight CTAs takes 8 (greedy) to 15 us (filters), of which each exchange
@@ -162,8 +162,8 @@ DS_DEV float2 weight_pair(const WeightMap& w, float l) {
 }
 
 // The exact weight in units. A call in the kernels for rows left, whose passes are mostly these
-// (256 x 262144 mixed: 224 us in all, 243 with copies in every pass, which spill); inlined in the
-// others (one row: 14.0 us, 14.6 with calls).
+// (256 x 262144 mixed: 224 us in all, 243 with copies in every pass, which spilled, as measured when
+// that was chosen); inlined in the others (one row: 14.0 us, 14.6 with calls).
 #ifdef DS_SAMPLE_WEIGHTS_CALLED
 #define DS_WEIGHT_FN __device__ __noinline__
 #else
